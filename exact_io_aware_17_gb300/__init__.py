@@ -233,27 +233,35 @@ def _need(name, t, shape, dtype, device):
                          f"the call's first tensor), got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _made(t, stream):
-    """A tensor that the call allocated: torch must not hand its memory on before `stream` is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape, dtype, device, stream):
+    """An output that the call allocates.  On a given stream it is of that stream's memory, where nothing that the caller's
+    stream still has queued can be using it, and torch hands it on only when the caller's stream is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
 def _output(name, t, shape, dtype, device, stream):
     """The caller's output tensor, checked, or a new one."""
     if t is None:
-        return _made(torch.empty(shape, dtype=dtype, device=device), stream)
+        return _new(shape, dtype, device, stream)
     _need(name, t, shape, dtype, device)
     return t
 
 
 def _check_workspace(workspace, need, device, stream):
-    """The caller's workspace, or one that torch allocates; (None, 0) where the call needs none."""
+    """The caller's workspace, or one of the call's stream that torch allocates; (None, 0) where the call needs none."""
     if workspace is None:
         if not need:
             return None, 0
-        workspace = _made(torch.empty(need, dtype=torch.uint8, device=device), stream)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
