@@ -122,14 +122,31 @@ def _check_tensor(name, t, shape, dtype, device=None):
         raise ValueError(f"{name}: on {t.device}, expected {device} (every tensor of a call on one GPU)")
 
 
+def _scratch(shape, dtype, device, stream):
+    """Memory that the call allocates: on a given stream, of that stream's pool, where nothing that the caller's stream
+    still has queued can be using it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream):
+    """An output that the call allocates: torch hands its memory on only when the caller's stream is done with it too."""
+    t = _scratch(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def fa_fwd(q, k, v, scale=None, o=None, lse=None, stream=None, _entry="fa_fwd"):
     """bf16 forward: returns (o bf16 [B,H,N,d], lse fp32 [B,H,N])."""
     B, H, N, d = _shape(q)
     dev = q.device
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_tensor(name, t, (B, H, N, d), torch.bfloat16, dev)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=dev) if lse is None else lse
+    o = _new((B, H, N, d), torch.bfloat16, dev, stream) if o is None else o
+    lse = _new((B, H, N), torch.float32, dev, stream) if lse is None else lse
     _check_tensor("o", o, (B, H, N, d), torch.bfloat16, dev)
     _check_tensor("lse", lse, (B, H, N), torch.float32, dev)
     with torch.cuda.device(dev):
@@ -149,8 +166,8 @@ def fa_fwd_f32(q, k, v, scale=None, o=None, lse=None, stream=None):
     dev = q.device
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_tensor(name, t, (B, H, N, d), torch.float32, dev)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=dev) if lse is None else lse
+    o = _new((B, H, N, d), torch.float32, dev, stream) if o is None else o
+    lse = _new((B, H, N), torch.float32, dev, stream) if lse is None else lse
     _check_tensor("o", o, (B, H, N, d), torch.float32, dev)
     _check_tensor("lse", lse, (B, H, N), torch.float32, dev)
     with torch.cuda.device(dev):
@@ -168,9 +185,9 @@ def fa_bwd(q, k, v, o, do, lse, scale=None, dq=None, dk=None, dv=None, workspace
     least fa_bwd_workspace_size(B,H,N,d) bytes; one is allocated by torch if not given."""
     B, H, N, d = _shape(q)
     dev = q.device
-    dq, dk, dv = _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv)
+    dq, dk, dv = _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv, stream)
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), dtype=torch.uint8, device=dev)
+        workspace = _scratch((fa_bwd_workspace_size(B, H, N, d),), torch.uint8, dev, stream)
     if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
     with torch.cuda.device(dev):
@@ -180,7 +197,7 @@ def fa_bwd(q, k, v, o, do, lse, scale=None, dq=None, dk=None, dv=None, workspace
     return dq, dk, dv
 
 
-def _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv):
+def _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv, stream):
     """Checks the backward's inputs and caller-given outputs (dtype, shape, contiguity, one device) and
     allocates the outputs not given."""
     B, H, N, d = _shape(q)
@@ -188,9 +205,9 @@ def _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv):
     for name, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do)):
         _check_tensor(name, t, (B, H, N, d), torch.bfloat16, dev)
     _check_tensor("lse", lse, (B, H, N), torch.float32, dev)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new((B, H, N, d), torch.bfloat16, dev, stream) if dq is None else dq
+    dk = _new((B, H, N, d), torch.bfloat16, dev, stream) if dk is None else dk
+    dv = _new((B, H, N, d), torch.bfloat16, dev, stream) if dv is None else dv
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _check_tensor(name, t, (B, H, N, d), torch.bfloat16, dev)
     return dq, dk, dv
@@ -203,7 +220,7 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, scale=None, dq=None, dk=None, dv=None, s
     raise FAError (FA_ERR_INVALID_ARG)."""
     B, H, N, d = _shape(q)
     dev = q.device
-    dq, dk, dv = _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv)
+    dq, dk, dv = _bwd_outputs(q, k, v, o, do, lse, dq, dk, dv, stream)
     with torch.cuda.device(dev):
         _check(load_library().fa_bwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                                              _ptr(dk), _ptr(dv), B, H, N, d, _default_scale(d, scale),
@@ -233,17 +250,6 @@ def _need(name, t, shape, dtype, device):
                          f"the call's first tensor), got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _new(shape, dtype, device, stream):
-    """An output that the call allocates.  On a given stream it is of that stream's memory, where nothing that the caller's
-    stream still has queued can be using it, and torch hands it on only when the caller's stream is done with it too."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
 def _output(name, t, shape, dtype, device, stream):
     """The caller's output tensor, checked, or a new one."""
     if t is None:
@@ -257,11 +263,7 @@ def _check_workspace(workspace, need, device, stream):
     if workspace is None:
         if not need:
             return None, 0
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _scratch((need,), torch.uint8, device, stream)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()

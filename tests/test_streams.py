@@ -55,9 +55,45 @@ def test_outputs_come_from_the_given_stream(streams):
 
 def test_the_workspace_comes_from_the_given_stream(streams):
     import exact_io_aware_17_gb300 as fa
-    assert fa._check_workspace(None, 64, "cuda:0", "side")[0].made_on == "side"
+    t = fa._check_workspace(None, 64, "cuda:0", "side")[0]
+    assert t.made_on == "side" and t.recorded == []        # the caller's stream never uses it
     assert fa._check_workspace(None, 64, "cuda:0", None)[0].made_on == "caller"
     assert fa._check_workspace(None, 0, "cuda:0", "side") == (None, 0)
+
+
+def test_the_square_calls_outputs_come_from_the_given_stream(streams, monkeypatch):
+    """Every output and workspace of fa_fwd, fa_fwd_f32 and the two backward calls."""
+    import exact_io_aware_17_gb300 as fa
+    made = []
+
+    def empty(*a, **kw):
+        made.append(_Tensor(streams[-1]))
+        return made[-1]
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, empty)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    for name, value in (("_check_tensor", lambda *a: None), ("_ptr", lambda t: None), ("_stream", lambda *a: None),
+                        ("load_library", Library), ("fa_bwd_workspace_size", lambda *a: 64)):
+        monkeypatch.setattr(fa, name, value)
+    x = torch.zeros(1, 1, 1, 64)
+    monkeypatch.setattr(_Tensor, "is_cuda", True, raising=False)
+    monkeypatch.setattr(_Tensor, "device", x.device, raising=False)
+    for call, outputs, others in ((lambda s: fa.fa_fwd(x, x, x, stream=s), 2, 0), (lambda s: fa.fa_fwd_f32(x, x, x, stream=s), 2, 0),
+                                  (lambda s: fa.fa_fwd_stepnorm(x, x, x, stream=s), 2, 0),
+                                  (lambda s: fa.fa_bwd(x, x, x, x, x, x, stream=s), 3, 1),
+                                  (lambda s: fa.fa_bwd_noalloc(x, x, x, x, x, x, stream=s), 3, 0)):
+        made.clear()
+        call("side")
+        assert [t.made_on for t in made] == ["side"] * (outputs + others)
+        assert [t.recorded for t in made] == [["caller"]] * outputs + [[]] * others
+        made.clear()
+        call(None)
+        assert [t.made_on for t in made] == ["caller"] * (outputs + others)
 
 
 # ------------------------------------------------------------------------------------------------ GPU
@@ -128,3 +164,16 @@ def test_cache_calls_on_another_stream(rows):
     tables = [table.clone() for _ in range(3)]          # a call changes its own
     sizes = _sizes(fa.fa_cache_plan(lens, new, tables.pop(), free, bs, 1000), 0)
     _apart(fa, lambda **kw: fa.fa_cache_plan(lens, new, tables.pop(), free, bs, 1000, **kw), sizes)
+
+
+@pytest.mark.gpu
+def test_square_attention_on_another_stream():
+    fa = need_gpu()
+    q, k, v, do = (_normal(2, 3, 500, 64) + i for i in range(4))
+    o, lse = fa.fa_fwd(q, k, v)
+    _apart(fa, lambda **kw: fa.fa_fwd(q, k, v, **kw), _sizes((o, lse), 0))
+    ws = fa.fa_bwd_workspace_size(2, 3, 500, 64)
+    _apart(fa, lambda **kw: fa.fa_bwd(q, k, v, o, do, lse, **kw)[1:], _sizes((q, k, v), ws))
+    _apart(fa, lambda **kw: fa.fa_bwd_noalloc(q, k, v, o, do, lse, **kw)[1:], _sizes((q, k, v), 0))
+    q, k, v = (x.float() for x in (q, k, v))
+    _apart(fa, lambda **kw: fa.fa_fwd_f32(q, k, v, **kw), _sizes(fa.fa_fwd_f32(q, k, v), 0))
