@@ -14,9 +14,10 @@
 // thread forms S of the next tile before P V of this one.  Four warps hold a row a lane: running maximum and sum, P to
 // tensor memory as f16.  Up to 64 rows stand in the lanes twice, and each copy takes half of a tile's keys (P of the others
 // is zero), with a maximum, sum and O of its own until the end, so that four warps share the softmax and not two.  Q is f16 too, scaled by a power of two per row, so that elements down to 2^-29 of the row's
-// largest are exact.  A key block's scale multiplies its scores, a value block's its probabilities, relative to the largest
-// value scale so far.  O is rescaled only when a row's maximum has grown by more than 2^8 (P then stays within f16's range
-// with 2^7 to spare for small ones).
+// largest are exact.  A key block's scale multiplies its scores, a value block's its probabilities: P is 2^(s + log2 scale - u),
+// with the row's running maximum u of s + log2 scale over the keys that it sees, as in fa_rows.cu.  O is rescaled only when u
+// has grown by more than 2^8 (P then stays within f16's range with 2^7 to spare for small ones; f16 drops what is below 2^-32 of
+// the row's largest).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,8 +39,9 @@ constexpr int kMmaWarp = 4, kFirstConverter = 5, kConverters = 8;   // warps; 0-
 constexpr int kStages = 3;        // tiles of K, and of V, in shared memory
 constexpr int kScaleSlots = 8;    // of tiles' scales: those of K are up to four tiles ahead of the softmax
 constexpr int kThreads = 32 * (kFirstConverter + kConverters);
-constexpr float kGrowth = 8.f;    // log2 units by which a maximum may grow before O follows
+constexpr float kGrowth = 8.f;    // log2 units by which a maximum may grow before l or O follows
 constexpr float kPScale = 128.f;  // of probabilities in f16: with 2^8 for the growth at most 2^15
+constexpr float kMaxFloat = 3.402823466e38f;
 
 struct CacheBarriers {
     uint64_t q_full;              // 128 arrivals
@@ -90,6 +92,10 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, int high) {
     if (high) asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
     else asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
     return r;
+}
+// log2 of a power of two (of 0: -127), from its exponent bits: 2^23 + them is exact.
+__device__ __forceinline__ float log2_scale(float x) {
+    return __uint_as_float(0x4b000000u | __float_as_uint(x) >> 23) - (8388608.f + 127.f);
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
@@ -291,7 +297,7 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
         // mul = 2^(14 - exponent of amax), kept a normal number.  A NaN among the elements is one in f16 too.
         const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 127);
         const float mul = __uint_as_float((uint32_t)(min(14 - ex, 100) + 127) << 23);
-        qscale = amax <= 3.402823466e38f ? a.scale_log2 / mul : __int_as_float(0x7fc00000);
+        qscale = amax <= kMaxFloat ? a.scale_log2 / mul : __int_as_float(0x7fc00000);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
             const uint4 w4 = mine ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
@@ -317,7 +323,7 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
     }
 
     const int limit = len - (a.N - 1 - row % a.N);   // keys that the row sees
-    float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f;   // vinv: kPScale / vref
+    float m = -INFINITY, l = 0.f, u = -INFINITY;   // l in units of 2^m, O in units of 2^u / kPScale
     constexpr bool kHold = chunks <= 2;   // the scores stay in registers between the maximum and the probabilities
     for (int j = 0; j < T; ++j) {
         const int s = j & 1, key0 = (i0 + j) * BN;
@@ -327,15 +333,12 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
         const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + j % kScaleSlots * 8;
         const float* vs = ks + kScaleSlots * 8;
         const uint32_t tS = tmem + lane_off + 128 * s;
-        float mx = m, vnew = vref;
+        float mx = m, ux = u;
         bool whole = key0 + BN <= limit_all;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            whole = whole && ks[u] >= 0.f;
-            vnew = fmaxf(vnew, vs[u]);
-        }
+        for (int i = 0; i < 8; ++i) whole = whole && ks[i] >= 0.f;
         // Scores are x * cs; in a tile that masks something, -inf or the scaled score, and cs is 1.
-        auto group_scale = [&](int u) { return whole ? qscale * ks[u] : 1.f; };
+        auto group_scale = [&](int i) { return whole ? qscale * ks[i] : 1.f; };
         auto mask = [&](uint32_t (&x)[32], int c) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -345,14 +348,16 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
         };
         auto largest = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int i = 0; i < 2; ++i) {
                 float g[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        g[k] = max3(g[k], __uint_as_float(x[16 * u + e + 2 * k]), __uint_as_float(x[16 * u + e + 2 * k + 1]));
-                mx = fmaxf(mx, fmaxf(g[0], g[1]) * group_scale(2 * c + u));
+                        g[k] = max3(g[k], __uint_as_float(x[16 * i + e + 2 * k]), __uint_as_float(x[16 * i + e + 2 * k + 1]));
+                const float s = fmaxf(g[0], g[1]) * group_scale(2 * c + i);
+                mx = fmaxf(mx, s);
+                ux = fmaxf(ux, s + log2_scale(vs[2 * c + i]));
             }
         };
         uint32_t held[kHold ? chunks : 1][32];
@@ -374,14 +379,16 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
                 largest(held[0], c);
             }
         }
-        // O follows the maximum and, with its unit, the largest value scale.
-        const bool grown = mx > m + kGrowth || (m == -INFINITY && mx > -INFINITY);
-        if (__any_sync(0xffffffffu, grown || vnew != vref)) {
-            const float alpha = !grown ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
+        if (mx > m + kGrowth || (m == -INFINITY && mx > -INFINITY)) {
+            l *= m == -INFINITY ? 0.f : ex2(m - mx);
+            m = mx;
+        }
+        const bool grown = ux > u + kGrowth || (u == -INFINITY && ux > -INFINITY);
+        if (__any_sync(0xffffffffu, grown)) {   // O follows its unit
             if (j > 0) {
                 if (!warp_wait(&bars->pv_done[s ^ 1], ((j - 1) >> 1) & 1, wc)) return;
                 tc_fence_after();
-                const float f = vnew > 0.f ? alpha * (vref / vnew) : 0.f;
+                const float f = !grown ? 1.f : u == -INFINITY ? 0.f : ex2(u - ux);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t x[32];
@@ -393,11 +400,9 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
                 }
                 tmem_st_wait();
             }
-            l *= alpha;
-            if (grown) m = mx;
-            vref = vnew;
-            vinv = vref > 0.f ? kPScale / vref : 0.f;
+            if (grown) u = ux;
         }
+        const float pscale = u == -INFINITY ? 0.f : ex2(m - u) * kPScale;
         // P's buffer is free: S of this tile was formed behind P V of the tile before the last.
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t nm2 = f2_pack(nm, nm);
@@ -405,18 +410,19 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
         auto probabilities = [&](const uint32_t (&x)[32], int c) {
             uint32_t pk[16];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float cs = group_scale(2 * c + u), pv = vs[2 * c + u] * vinv;
+            for (int i = 0; i < 2; ++i) {
+                // (pv is beyond fp32 only where a probability that would matter is 0 in fp32.)
+                const float cs = group_scale(2 * c + i), pv = fminf(vs[2 * c + i] * pscale, kMaxFloat);
                 const uint64_t cs2 = f2_pack(cs, cs), pv2 = f2_pack(pv, pv);
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     float x0, x1;
-                    f2_unpack(ffma2(f2_pack(__uint_as_float(x[16 * u + e]), __uint_as_float(x[16 * u + e + 1])), cs2, nm2), x0, x1);
+                    f2_unpack(ffma2(f2_pack(__uint_as_float(x[16 * i + e]), __uint_as_float(x[16 * i + e + 1])), cs2, nm2), x0, x1);
                     const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
                     l2 = fadd2(l2, p2);
                     float p0, p1;
                     f2_unpack(fmul2(p2, pv2), p0, p1);
-                    pk[8 * u + e / 2] = f16x2(p0, p1);
+                    pk[8 * i + e / 2] = f16x2(p0, p1);
                 }
             }
             tmem_st16(tmem + lane_off + C::kColP + 64 * s + 16 * c, pk);
@@ -446,8 +452,8 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
         tc_fence_after();
     }
     const int split = blockIdx.x / a.row_tiles % a.splits, rt = blockIdx.x % a.row_tiles;
-    // O is in units of vref / kPScale; the copies of a row join through the K and V buffers, which are free by now.
-    float unit = vref / kPScale;
+    // The copies of a row join through the K and V buffers, which are free by now.
+    const float unit = u == -INFINITY ? 0.f : ex2(u - m) / kPScale;
     constexpr int kPitch = D + 4;
     float* joint = reinterpret_cast<float*>(smem + C::kOffKV);
     float2* joint_ml = reinterpret_cast<float2*>(joint + BM * kPitch);
@@ -464,7 +470,7 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(joint + r * kPitch + 32 * c + e) =
-                    T > 0 && vref > 0.f ? make_float4(__uint_as_float(x[e]) * unit, __uint_as_float(x[e + 1]) * unit,
+                    T > 0 ? make_float4(__uint_as_float(x[e]) * unit, __uint_as_float(x[e + 1]) * unit,
                                                       __uint_as_float(x[e + 2]) * unit, __uint_as_float(x[e + 3]) * unit)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -511,7 +517,7 @@ __device__ void cache_row(const CacheTcArgs& a, uint8_t* smem, CacheBarriers* ba
                 tmem_ld_wait();
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = T > 0 && vref > 0.f ? __float_as_uint(__uint_as_float(x[e]) * (unit * inv)) : 0u;
+            for (int e = 0; e < 32; ++e) x[e] = T > 0 ? __float_as_uint(__uint_as_float(x[e]) * (unit * inv)) : 0u;
         }
         if (bars->new_nan) {   // the newest tokens' NaN, where this row sees them
             for (int key = max(limit_all, i0 * BN); key < min(limit, i1 * BN); ++key) {

@@ -21,9 +21,10 @@
 // largest, which are off by up to 2^-22 of it.  Its sums measured exact to 2^-21 of their terms' magnitudes.  The two pieces
 // are the two halves of M.  9 to 16 rows would need both products, so K's codes become f16 (exact) and Q too, scaled by a
 // power of two per row (exact down to 2^-29 of the row's largest): 64 requests x 8192 tokens x 8 heads, d = 128, took 168
-// us with two e4m3 products and 140 so (5.7 TB/s), d = 64 over full lengths 127 and 107.  V's codes become f16 (exact) for P V, which rounds P
-// to 11 bits and drops what is below 2^-37 of the row's largest.  The scale of a key block multiplies its scores, that of a value block
-// its probabilities, relative to the largest value scale so far.
+// us with two e4m3 products and 140 so (5.7 TB/s), d = 64 over full lengths 127 and 107.  V's codes become f16 (exact) for P V.  The scale of a key block multiplies its scores, that of a value block its
+// probabilities: the product takes 2^(s + log2 scale - u) as f16, with the row's running maximum u of s + log2 scale over the
+// keys that it sees, so that a block counts by what it adds to the row, however far the scales lie apart and whatever other rows
+// see.  f16 rounds this to 11 bits and drops what is below 2^-37 of the row's largest.
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -51,6 +52,7 @@ __host__ __device__ constexpr int ring_bytes(int d, bool small, bool cache) {
 }
 constexpr float kLoScale = 32.f;      // hi's last place is at most 16, so lo is at most 8 before this scale (codes reach 448)
 constexpr float kPScale = 4096.f;     // probabilities in f16: 2^12 keeps them out of the subnormals
+constexpr float kMaxFloat = 3.402823466e38f;
 
 struct RowsArgs {
     const __nv_bfloat16* q;           // [BH][R][D]
@@ -137,6 +139,10 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
+}
+// log2 of a power of two (of 0: -127), from its exponent bits: 2^23 + them is exact.
+__device__ __forceinline__ float log2_scale(float x) {
+    return __uint_as_float(0x4b000000u | __float_as_uint(x) >> 23) - (8388608.f + 127.f);
 }
 // Code i of w as a float.
 __device__ __forceinline__ float e4m3_f32(uint32_t w, int i) {
@@ -329,7 +335,7 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
                 const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 127);
                 const float mul = __uint_as_float((uint32_t)(min((kSmall ? 7 : 14) - ex, 100) + 127) << 23);
                 // An infinity or NaN in the row makes all of its scores NaN, as the product would (but for zeros).
-                qscale[e] = amax <= 3.402823466e38f ? a.scale_log2 / mul : __int_as_float(0x7fc00000);
+                qscale[e] = amax <= kMaxFloat ? a.scale_log2 / mul : __int_as_float(0x7fc00000);
 #pragma unroll
                 for (int i = 0; i < kQ8; ++i) {
                     const uint32_t w[4] = {raw[e][i].x, raw[e][i].y, raw[e][i].z, raw[e][i].w};
@@ -381,8 +387,13 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
         m[e] = -INFINITY;
         l[e] = 0.f;
     }
-    // Cache: the largest value scale so far (O is in units of vref / kPScale), and kPScale / vref.
-    float vref = 0.f, vinv = 0.f;
+    // Cache: um, the running maximum of score + log2 of the value scale (O is in units of 2^um / kPScale), and kPScale 2^(m - um).
+    float um[kE], pscale[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        um[e] = -INFINITY;
+        pscale[e] = 0.f;
+    }
     const bool odd = t & 1;
     // Byte pairs of two keys side by side, whichever order a lane loaded them in.
     const uint32_t sel_lo = kCache ? (odd ? 0x1504u : 0x5140u) : (odd ? 0x1054u : 0x5410u);
@@ -466,51 +477,58 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) cs[e][0] = cs[e][1] = 1.f;
         }
-        float alpha[kE];
+        float m_new[kE], um_new[kE];
         bool moved = false;
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
             float mu[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int j = 0; j < T::kNT; ++j) mu[j / 2] = max3(mu[j / 2], sc[j][2 * e], sc[j][2 * e + 1]);
-            float mx = T::kNT > 2 ? max3(m[e], mu[0] * cs[e][0], mu[1] * cs[e][1]) : fmaxf(m[e], mu[0] * cs[e][0]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            moved |= mx != m[e];
-            alpha[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - mx);
-            m[e] = mx;
+            m_new[e] = T::kNT > 2 ? max3(m[e], mu[0] * cs[e][0], mu[1] * cs[e][1]) : fmaxf(m[e], mu[0] * cs[e][0]);
+            um_new[e] = um[e];
+            if (kCache)
+                um_new[e] = max3(um[e], fmaf(mu[0], cs[e][0], log2_scale(vs[0])), fmaf(mu[1], cs[e][1], log2_scale(vs[1])));
+            moved |= m_new[e] != m[e] || (kCache && um_new[e] != um[e]);
         }
-        const float vnew = kCache ? max3(vref, vs[0], vs[1]) : vref;
-        if (__any_sync(0xffffffffu, moved || vnew != vref)) {
-            // O follows the maximum and, with its unit, the largest value scale; l follows the maximum.
+        if (__any_sync(0xffffffffu, moved)) {   // l follows the maximum, O its unit (bf16 keys: the maximum)
+            float fall[kE];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+#pragma unroll
+                for (int o = 1; o <= 2; ++o) {   // the other keys' lanes of the row
+                    m_new[e] = fmaxf(m_new[e], __shfl_xor_sync(0xffffffffu, m_new[e], o));
+                    if (kCache) um_new[e] = fmaxf(um_new[e], __shfl_xor_sync(0xffffffffu, um_new[e], o));
+                }
+                const float alpha = m[e] == -INFINITY ? 0.f : ex2(m[e] - m_new[e]);
+                l[e] *= alpha;
+                m[e] = m_new[e];
+                fall[e] = alpha;
+                if (kCache) {
+                    fall[e] = um[e] == -INFINITY ? 0.f : ex2(um[e] - um_new[e]);
+                    um[e] = um_new[e];
+                    pscale[e] = um[e] == -INFINITY ? 0.f : ex2(m[e] - um[e]) * kPScale;
+                }
+            }
             float al[2];
             if constexpr (kSmall) {   // O's rows are 2t and 2t + 1; lane 4 r holds row r's
-                al[0] = __shfl_sync(0xffffffffu, alpha[0], 8 * t);
-                al[1] = __shfl_sync(0xffffffffu, alpha[0], 8 * t + 4);
+                al[0] = __shfl_sync(0xffffffffu, fall[0], 8 * t);
+                al[1] = __shfl_sync(0xffffffffu, fall[0], 8 * t + 4);
             } else {
-                al[0] = alpha[0];
-                al[1] = alpha[kE - 1];
-            }
-            if (kCache && vnew != vref) {
-                const float r = vref / vnew;
-                al[0] *= r;
-                al[1] *= r;
-                vref = vnew;
-                vinv = kPScale / vnew;
+                al[0] = fall[0];
+                al[1] = fall[kE - 1];
             }
 #pragma unroll
             for (int s = 0; s < kAcc; ++s)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[s][c] *= al[kSmall ? c & 1 : c >> 1];
-#pragma unroll
-            for (int e = 0; e < kE; ++e) l[e] *= alpha[e];
         }
-        const float pv[2] = {kCache ? vs[0] * vinv : 1.f, kCache ? vs[1] * vinv : 1.f};
         uint32_t pa[T::kKeys / 16][2 * kE];   // [.][2 (8-key half) + e] as the A operand, or [8-key half] as the B operand
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
             const float nm = m[e] == -INFINITY ? 0.f : -m[e];
             const uint64_t nm2 = f2_pack(nm, nm);
+            // (Beyond fp32 only where a probability that would matter is 0 in fp32.)
+            const float pv[2] = {kCache ? fminf(vs[0] * pscale[e], kMaxFloat) : 1.f, kCache ? fminf(vs[1] * pscale[e], kMaxFloat) : 1.f};
             uint64_t l2 = 0;
 #pragma unroll
             for (int j = 0; j < T::kNT; ++j) {
@@ -631,7 +649,14 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
     auto col = [](int d) { return d + 4 * (d / 16); };
     float* so = reinterpret_cast<float*>(smem);
     float2* sml = reinterpret_cast<float2*>(so + kWarps * kWarpPitch);
-    const float unit = kCache ? vref / kPScale : 1.f;
+    float unit[2] = {1.f, 1.f};   // of O's rows, as fall above
+    if constexpr (kCache) {
+        float own[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) own[e] = um[e] == -INFINITY ? 0.f : ex2(um[e] - m[e]) / kPScale;
+        unit[0] = kSmall ? __shfl_sync(0xffffffffu, own[0], 8 * t) : own[0];
+        unit[1] = kSmall ? __shfl_sync(0xffffffffu, own[0], 8 * t + 4) : own[kE - 1];
+    }
     float* mine = so + warp * kWarpPitch;
     if constexpr (kSmall) {
         constexpr int kTilesPerWord = kCache ? 2 : 1;
@@ -641,7 +666,7 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
             for (int c = 0; c < 2; ++c)
                 *reinterpret_cast<float2*>(mine + (2 * t + c) * kRowPitch +
                                            col(T::column(w / kTilesPerWord, g) + 2 * (w % kTilesPerWord))) =
-                    make_float2(acc[w][c] * unit, acc[w][2 + c] * unit);
+                    make_float2(acc[w][c] * unit[c], acc[w][2 + c] * unit[c]);
     } else {
         constexpr int kCols = 4 / T::kElt;   // columns of a word of V
 #pragma unroll
@@ -651,7 +676,7 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
 #pragma unroll
                 for (int s = 0; s < kAcc; s += 2)
                     *reinterpret_cast<float2*>(mine + (g + 8 * e) * kRowPitch + col(T::column(s / kCols, 2 * t + c) + s % kCols)) =
-                        make_float2(acc[s][2 * e + c] * unit, acc[s + 1][2 * e + c] * unit);
+                        make_float2(acc[s][2 * e + c] * unit[e], acc[s + 1][2 * e + c] * unit[e]);
     }
     if (t == 0) {
 #pragma unroll

@@ -224,6 +224,10 @@ fa_status fa_cache_append(const void* k, const void* v, const long long* slots, 
  *           N new tokens has its rows at the end).  Table entries outside [0, n_blocks) hold no tokens: their
  *           places are masked.  What the blocks hold behind a request's tokens is not used.
  *   workspace : as fa_cross_fwd's, fa_cache_fwd_workspace_size(...) bytes.
+ * Precision: each probability times its block's value scale is rounded to f16 relative to the largest such product of its
+ * row: 11 bits, fewer below 2^-21 of the largest, nothing below 2^-32 (up to 32 rows Hq/Hk*N: 2^-26 and 2^-37).  So blocks
+ * may have scales as far apart as fa_cache_append makes them, and what a row does not see leaves it as it is.
+ * Probabilities below 2^-126 of a row's largest are 0.
  * Made for few rows: the cache is read once for up to 16 rows Hq/Hk*N of a key head (in larger calls, up to 128).
  * Repeatability: the same inputs give the same bits on every call.
  */
