@@ -375,7 +375,7 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, dev):
 
 def fa_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     """Puts the new tokens' keys and values (bf16 [T, Hk, d]; any token and head strides that are multiples of 8
-    elements, the last dimension contiguous) into their slots (int64 [T]) of the cache: k_cache, v_cache
+    elements, those of a single token or head whatever they are, the last dimension contiguous) into their slots (int64 [T]) of the cache: k_cache, v_cache
     float8_e4m3fn [n_blocks, Hk, block_size, d] and k_scale, v_scale fp32 [n_blocks, Hk], all in place."""
     dev = k.device
     n_blocks, H, bs, d = _check_cache(k_cache, v_cache, k_scale, v_scale, dev)

@@ -203,6 +203,9 @@ fa_status fa_cache_append(const void* k, const void* v, const long long* slots, 
     if (T < 0 || T > INT32_MAX - 1024) return set_error(FA_ERR_INVALID_ARG, "%s: T must be in [0, 2^31 - 1025] (got %d)", fn, T);
     fa_status st = check_cache(fn, H, d, n_blocks, block_size);
     if (st) return st;
+    // Strides of a single token or head are never used.
+    if (T <= 1) k_token_stride = v_token_stride = 0;
+    if (H == 1) k_head_stride = v_head_stride = 0;
     const long long strides[] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
     for (long long s : strides)
         if (s < 0 || s % 8) return set_error(FA_ERR_INVALID_ARG, "%s: strides must be >= 0 and multiples of 8 (got %lld)", fn, s);

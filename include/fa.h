@@ -202,7 +202,8 @@ fa_status fa_cache_plan(const int* lens, const int* new_lens, int* block_table, 
 /*
  * fa_cache_append — rounds new tokens' keys and values to e4m3 and puts them into their slots.
  *   k, v  : const bf16, T tokens of H heads of d values; element (t, h, c) is at t * token_stride + h * head_stride
- *           + c (strides in elements, multiples of 8; the pointers 16-byte aligned)
+ *           + c (strides in elements, multiples of 8, whatever they are for a single token or head; the pointers 16-byte
+ *           aligned)
  *   slots : const long long [T]; tokens with a slot outside [0, n_blocks * block_size) are skipped.  The tokens of
  *           one block must stand next to each other, in order and without gaps (as fa_cache_plan leaves them): if
  *           a block's tokens are scattered over the call, or a slot comes twice, that block's values are undefined.
