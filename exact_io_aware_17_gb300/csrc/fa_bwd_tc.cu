@@ -642,7 +642,7 @@ template <int D, bool kCross, bool kDirect>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-              const __grid_constant__ CUtensorMap tm_dq, const float* __restrict__ lse2, const float* __restrict__ row_d, float* __restrict__ dq_acc,
+              const __grid_constant__ CUtensorMap tm_dq, const float* lse2, const float* row_d, float* __restrict__ dq_acc,
               __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, int N, int Npad,
               int blocks_per_head, float scale, float scale_log2, long long wait_budget, int starve, BwdCross ca) {
     using C = BwdCfg<D>;
@@ -1102,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 bwd_walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                 const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
-                const float* __restrict__ lse2, const float* __restrict__ row_d, float* __restrict__ dq_acc,
+                const float* lse2, const float* row_d, float* __restrict__ dq_acc,
                 __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, int N, int Npad, float scale,
                 float scale_log2, long long wait_budget, int starve, BwdCross ca) {
     using C = WalkCfg<D, kNq>;
@@ -1278,17 +1278,25 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
     reinterpret_cast<uint2*>(dk)[idx] = k;
 }
 
-// dQ = bf16(scale * accumulator), four elements per thread, grid-stride.
-__global__ void bwd_dq_convert_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __restrict__ dq, float scale,
-                                      int64_t n4) {
+// dQ = bf16(scale * accumulator), four elements per thread and load, grid-stride.  The kernel ahead still adds to the
+// accumulator when this one starts, so it is not read-only memory: no __restrict__, plain loads from L2, and kLoads of them in
+// flight by hand.
+__global__ void bwd_dq_convert_kernel(const float* dq_acc, __nv_bfloat16* __restrict__ dq, float scale, int64_t n4) {
+    constexpr int kLoads = 4;
     griddep_wait();   // launched to start while the main kernel finishes: its reduce-adds must be complete
-    for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < n4;
-         idx += (int64_t)gridDim.x * blockDim.x) {
-        const float4 a = reinterpret_cast<const float4*>(dq_acc)[idx];
-        uint2 out;
-        out.x = pack_bf16(a.x * scale, a.y * scale);
-        out.y = pack_bf16(a.z * scale, a.w * scale);
-        reinterpret_cast<uint2*>(dq)[idx] = out;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n4; i0 += kLoads * step) {
+        float4 a[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            if (i0 + u * step < n4) a[u] = __ldcg(reinterpret_cast<const float4*>(dq_acc) + i0 + u * step);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            uint2 out;
+            out.x = pack_bf16(a[u].x * scale, a[u].y * scale);
+            out.y = pack_bf16(a[u].z * scale, a[u].w * scale);
+            if (i0 + u * step < n4) reinterpret_cast<uint2*>(dq)[i0 + u * step] = out;
+        }
     }
 }
 

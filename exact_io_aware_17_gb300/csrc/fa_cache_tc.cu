@@ -102,9 +102,13 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// (Not the read-only path: an append ahead on the stream may still be writing when this kernel starts.)
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
     return r;
 }
 // Codes that are NaN (all bits but the sign) become zero; *any says that there was one.
