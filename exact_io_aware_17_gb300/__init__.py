@@ -375,8 +375,9 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, dev):
 
 def fa_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     """Puts the new tokens' keys and values (bf16 [T, Hk, d]; any token and head strides that are multiples of 8
-    elements, those of a single token or head whatever they are, the last dimension contiguous) into their slots (int64 [T]) of the cache: k_cache, v_cache
-    float8_e4m3fn [n_blocks, Hk, block_size, d] and k_scale, v_scale fp32 [n_blocks, Hk], all in place."""
+    elements, those of a single token or head whatever they are, the last dimension contiguous) into their slots (int64
+    [T]) of the cache: k_cache, v_cache float8_e4m3fn [n_blocks, Hk, block_size, d] and k_scale, v_scale fp32 [n_blocks,
+    Hk], all in place."""
     dev = k.device
     n_blocks, H, bs, d = _check_cache(k_cache, v_cache, k_scale, v_scale, dev)
     if slots.dim() != 1:
@@ -450,6 +451,7 @@ def fa_last_error_string() -> str:
 
 
 __all__ = ["fa_fwd", "fa_fwd_stepnorm", "fa_fwd_f32", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_noalloc",
-           "fa_cross_fwd", "fa_cross_fwd_workspace_size", "fa_cross_bwd", "fa_cross_bwd_workspace_size", "fa_cache_plan", "fa_cache_append", "fa_cache_fwd",
-           "fa_cache_fwd_workspace_size", "fa_check_status", "fa_last_error_string", "fa_kernel_launches", "fa_test_force_wait_timeout",
-           "fa_debug_time_bwd_main", "load_library", "FAError", "EXPORTS", "LIB_PATH"]
+           "fa_cross_fwd", "fa_cross_fwd_workspace_size", "fa_cross_bwd", "fa_cross_bwd_workspace_size", "fa_cache_plan",
+           "fa_cache_append", "fa_cache_fwd", "fa_cache_fwd_workspace_size", "fa_check_status", "fa_last_error_string",
+           "fa_kernel_launches", "fa_test_force_wait_timeout", "fa_debug_time_bwd_main", "load_library", "FAError", "EXPORTS",
+           "LIB_PATH"]

@@ -50,8 +50,8 @@
 // second warpgroup's blocks have a buffer of their own, which the TMA thread adds only after it has issued
 // that dO load: with the second half's reduce issued first (from that warpgroup's own leader thread) the dO
 // tile queued behind it in the copy unit, which cost 11 % of the backward at d = 128.  At the end the K and V
-// tiles' space takes the bf16 rows of dK and dV, so that they leave in whole-row stores.  The kernel has no static shared memory, so its dynamic region starts aligned and
-// needs no slack.
+// tiles' space takes the bf16 rows of dK and dV, so that they leave in whole-row stores.  The kernel has no static
+// shared memory, so its dynamic region starts aligned and needs no slack.
 //
 // kCross (fa_cross_bwd): N counts keys, the queries are Tq blocks of their own length, and an entry has klen <= N
 // keys.  Grouped query heads that share a key head are rows of one head here, so dK and dV sum over the group
@@ -1190,8 +1190,8 @@ bwd_walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 }
 
 // -D_i = -(dO_i . O_i) and -LSE2_i = -LSE_i log2(e) into [head][Npad] arrays (pad rows: 0 and -inf);
-// zeroes n4 times four floats of the dQ accumulator (all of it, or none).  D/8 threads share a row (16-byte loads of O and dO), each warp takes
-// 2 * 32 / (D/8) rows per pass, so enough bytes are in flight to stream at HBM speed.
+// zeroes n4 times four floats of the dQ accumulator (all of it, or none).  D/8 threads share a row (16-byte loads of O and
+// dO), each warp takes 2 * 32 / (D/8) rows per pass, so enough bytes are in flight to stream at HBM speed.
 template <int D>
 __global__ void bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                                 const float* __restrict__ lse, float* __restrict__ row_d, float* __restrict__ lse2,

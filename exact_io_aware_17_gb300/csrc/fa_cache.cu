@@ -186,9 +186,10 @@ __device__ __forceinline__ float block_scale(float amax) {
 
 // One warp takes one run (tokens next to each other in the packed order and in one block) of one head, keys or
 // values: the largest magnitude first, then the codes; the values of short runs stay in registers between the two
-// passes, longer ones are read again from L2.  Lanes hold 8 values each (16-byte loads).  Bound by HBM: prompts of 131072
-// tokens x 8 heads of 128 take 67 us (6.0 TB/s read and written), 16 ragged ones of up to 2048 tokens 21 to 28 us for
-// blocks of 16 to 128 tokens (4.8 to 3.6 TB/s), 256 single tokens 5.8 us.  Holding 16 loads instead of 8 (24.0 against 22.5
+// passes, longer ones are read again from L2.  Lanes hold 8 values each (16-byte loads).  Bound by HBM: prompts of 65536
+// tokens x 8 heads of 128 in blocks of 16 take 66 us (6.1 TB/s read and written), of 131072 128 us (6.3; blocks of 32, 64 and
+// 128: 142, 131, 182), 16 ragged ones of up to 2048 tokens 21 to 28 us for blocks of 16 to 128 tokens (4.8 to 3.6 TB/s), 256
+// single tokens 5.8 us.  Holding 16 loads instead of 8 (24.0 against 22.5
 // us in blocks of 32) and a CTA a run instead of a warp (26.7 against 28.4 us in blocks of 128, 26.2 against 24.6 in
 // blocks of 64) were not worth it.
 template <int D>

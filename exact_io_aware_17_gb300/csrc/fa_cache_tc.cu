@@ -5,19 +5,21 @@
 //
 // The warps' streams of fa_rows.cu read and unpack the cache once for every 16 rows and are bound by that.  Here a CTA takes
 // up to 128 rows of a key head as the M of tcgen05 products: the cache is read and unpacked once, so the bound is HBM
-// again, nearly.  64 requests x 8192 tokens x 8 heads, d = 128, us in streams and here: 48 rows 410, 315 (3.4 TB/s), 64
-// rows 517, 317, 128 rows 984, 443.  A tile takes 1.0 us, the row warps' chain from S to P, where HBM would
+// again, nearly.  64 requests of 8192 tokens each x 8 heads (1.07 GB), d = 128, us in streams and here: 48 rows 425, 296
+// (3.6 TB/s), 64 rows 535, 299, 128 rows 1019, 424.  A tile takes 1.0 us, the row warps' chain from S to P, where HBM would
 // take 0.73; set-up and write-out of a CTA take 7 us, which only one CTA an SM does not overlap.
 //
 // Eight warps convert: each loads the codes of 32 of a tile's 128 keys or values two tiles ahead into registers, turns them
 // into f16 (exact) and writes them to shared memory in the products' layout, three tiles of 64 KB (K and V, d = 128).  A
 // thread forms S of the next tile before P V of this one.  Four warps hold a row a lane: running maximum and sum, P to
 // tensor memory as f16.  Up to 64 rows stand in the lanes twice, and each copy takes half of a tile's keys (P of the others
-// is zero), with a maximum, sum and O of its own until the end, so that four warps share the softmax and not two.  Q is f16 too, scaled by a power of two per row, so that elements down to 2^-29 of the row's
-// largest are exact.  A key block's scale multiplies its scores, a value block's its probabilities: P is 2^(s + log2 scale - u),
-// with the row's running maximum u of s + log2 scale over the keys that it sees, as in fa_rows.cu.  O is rescaled only when u
-// has grown by more than 2^8 (P then stays within f16's range with 2^7 to spare for small ones; f16 drops what is below 2^-32 of
-// the row's largest).
+// is zero), with a maximum, sum and O of its own until the end, so that four warps share the softmax and not two.  Q is f16
+// too, scaled by a power of two per row, so that elements down to 2^-29 of the row's largest are exact.
+//
+// A key block's scale multiplies its scores, a value block's its probabilities: P is 2^(s + log2 scale - u), with the row's
+// running maximum u of s + log2 scale over the keys that it sees, as in fa_rows.cu.  O is rescaled only when u has grown by
+// more than 8 (P then stays within f16's range with 2^7 to spare for small ones; f16 drops what is below 2^-32 of the row's
+// largest).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -80,11 +80,12 @@ fa_status check_cache_fwd(const char* fn, int B, int Hq, int Hk, int N, int d, i
     return FA_OK;
 }
 
-// More rows a key head than two of a stream's 16 go to the tensor-core tiles where there are two tiles of 128 keys an SM or more.
-// Streamed and tiled, us, at rows 32, 48, 64, 128: 64 requests x 8192 tokens x 8 heads, d = 128: 278, 285; 410, 315; 517, 317; 984, 443;
-// d = 64: 184, 228; 270, 247; 336, 249; 638, 395; 16 x 1024 x 8, d = 128: 20.6, 16.7; 21.8, 17.3; 31.4, 17.9; 49.2, 22.2;
-// 1 x 16384 x 4: 13.9, 16.4; 17.0, 16.7; 18.5, 17.6; 27.2, 22.6; 64 x 512 x 8: 33.4, 45.6; 47.7, 46.7; 59.6, 48.7; 110, 58.6; 1 x
-// 1000 x 8 (64 tiles): 10.7, 16.0; 10.9, 16.6; 11.4, 17.1; 11.7, 22.2.
+// More rows a key head than two of a stream's 16 go to the tensor-core tiles where there are two tiles of 128 keys an SM or
+// more.  Streamed and tiled, us, at rows 32, 48, 64, 128 of query heads (one token a request, requests of equal length): 64
+// requests x 8192 tokens x 8 heads, d = 128: 288, 293; 425, 296; 535, 299; 1019, 424; d = 64: 186, 240; 274, 241; 338, 243; 643,
+// 388; 16 x 1024 x 8, d = 128: 21.4, 15.8; 22.2, 16.5; 32.0, 17.0; 50.3, 21.1; 1 x 16384 x 4: 13.2, 15.4; 16.7, 16.2; 18.5,
+// 16.8; 27.4, 21.7; 64 x 512 x 8: 34.0, 43.9; 47.8, 46.7; 60.2, 48.8; 111, 56.5; 1 x 1000 x 8 (64 tiles): 10.2, 15.1; 10.3,
+// 15.8; 10.6, 16.2; 11.2, 20.6.  (The rule looks at rows and keys; rows that are new tokens have not been measured apart.)
 bool cache_in_tiles(int64_t bh, int R, int64_t keys) {
     return R > 2 * kMaxStreamRows && bh * ((keys + 127) / 128) >= 2 * kPlanSms;
 }

@@ -794,7 +794,8 @@ cudaError_t launch(const void* q, const void* k, const void* v, void* o, float* 
     const int T_all = (Nk + BN - 1) / BN;
     // (Clusters beyond a wave do not pay for ragged lengths either: 4 x 16 heads of 509 rows x up to 2047 keys of d = 64,
     // 128 pairs, took 25.3 us unsplit and 31.4 us split.)
-    const bool split_tail = !kStepNorm && !C::kHalf && (!kCross || ca.parts == 1) && T_all >= (kCross ? kClusterBlocks : 2) && rest > 0 && 2 * rest <= sms;
+    const bool split_tail = !kStepNorm && !C::kHalf && (!kCross || ca.parts == 1) &&
+                            T_all >= (kCross ? kClusterBlocks : 2) && rest > 0 && 2 * rest <= sms;
     const bool parts = kCross && ca.parts > 1;
     const unsigned grid = (unsigned)(split_tail || parts ? full : pairs);
     const float scale_log2 = scale * 1.4426950408889634f;

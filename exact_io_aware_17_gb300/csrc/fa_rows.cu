@@ -20,11 +20,12 @@
 // a power-of-two scale per row: 4 + 4 significant bits hold a bf16 exactly, but for elements below 2^-14 of the row's
 // largest, which are off by up to 2^-22 of it.  Its sums measured exact to 2^-21 of their terms' magnitudes.  The two pieces
 // are the two halves of M.  9 to 16 rows would need both products, so K's codes become f16 (exact) and Q too, scaled by a
-// power of two per row (exact down to 2^-29 of the row's largest): 64 requests x 8192 tokens x 8 heads, d = 128, took 168
-// us with two e4m3 products and 140 so (5.7 TB/s), d = 64 over full lengths 127 and 107.  V's codes become f16 (exact) for P V.  The scale of a key block multiplies its scores, that of a value block its
-// probabilities: the product takes 2^(s + log2 scale - u) as f16, with the row's running maximum u of s + log2 scale over the
-// keys that it sees, so that a block counts by what it adds to the row, however far the scales lie apart and whatever other rows
-// see.  f16 rounds this to 11 bits and drops what is below 2^-37 of the row's largest.
+// power of two per row (exact down to 2^-29 of the row's largest): 64 requests of 4096 to 8192 tokens x 8 heads (806 MB),
+// d = 128, took 168 us with two e4m3 products and 140 so (5.7 TB/s), and of 8192 tokens each, d = 64, 127 and 107.  V's codes
+// become f16 (exact) for P V.  The scale of a key block multiplies its scores, that of a value block its probabilities: the
+// product takes 2^(s + log2 scale - u) as f16, with the row's running maximum u of s + log2 scale over the keys that it sees,
+// so that a block counts by what it adds to the row, however far the scales lie apart and whatever other rows see.  f16 rounds
+// this to 11 bits and drops what is below 2^-37 of the row's largest.
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -40,8 +41,8 @@ using namespace ptx;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs an SM, as the registers allow, and the ring of each of their warps, which together fill its shared memory.  Measured at
-// 2 (24 KB), 3 (16 KB) and 4 (12 KB) CTAs, us, for 64 x 8192 tokens x 8 heads: d = 128, 4 rows a head 130, 126, -; 16 rows 140,
-// 136, -; d = 64, 4 rows 91, 78, 73; 16 rows over full lengths -, 107, 103, but one request of 131072 tokens x 4 heads 21.2,
+// 2 (24 KB), 3 (16 KB) and 4 (12 KB) CTAs, us, for 64 x 4096 to 8192 tokens x 8 heads: d = 128, 4 rows a head 130, 126, -; 16
+// rows 140, 136, -; d = 64, 4 rows 91, 78, 73; 16 rows over 8192 tokens each -, 107, 103, but one request of 131072 tokens x 4 heads 21.2,
 // 22.9.  Bf16 keys, 64 heads x 32768, d = 128: 153, 150; 16 rows: 128 heads x 1000 13.0, 15.5, 512 x 8192 309, 305; 32 x 4096 x
 // 16 heads, d = 64: 45.3, 43.9, 43.4.
 __host__ __device__ constexpr int ctas_per_sm(int d, bool small, bool cache) {
@@ -528,7 +529,8 @@ rows_kernel(const __grid_constant__ RowsArgs a) {
             const float nm = m[e] == -INFINITY ? 0.f : -m[e];
             const uint64_t nm2 = f2_pack(nm, nm);
             // (Beyond fp32 only where a probability that would matter is 0 in fp32.)
-            const float pv[2] = {kCache ? fminf(vs[0] * pscale[e], kMaxFloat) : 1.f, kCache ? fminf(vs[1] * pscale[e], kMaxFloat) : 1.f};
+            const float pv[2] = {kCache ? fminf(vs[0] * pscale[e], kMaxFloat) : 1.f,
+                                 kCache ? fminf(vs[1] * pscale[e], kMaxFloat) : 1.f};
             uint64_t l2 = 0;
 #pragma unroll
             for (int j = 0; j < T::kNT; ++j) {
@@ -845,9 +847,9 @@ RowsPlan rows_plan(int64_t bh, int R, int d, int64_t keys, int tile_keys) {
     // Few items: one wave of splits, of 128 KB of keys and values or more (16 heads x 512 bf16 keys of d =
     // 64 took 5 us either way, and a second kernel costs the host 6); where they leave slots idle and the splits stay
     // long, two to four fuller waves.  Many items: a few waves, which balance ragged lengths, of at least 32 tiles a CTA.
-    // Measured with two CTAs an SM, us at splits for 1, 2, 4 and 8 waves: one request of 131072 tokens x 4 heads (4 items) 31, 39, 56, 74; 8 x 2000
-    // tokens x 8 heads (64 items) 15.4, 15.8, 15.7, 16.0 (19.6 at 32 tiles a CTA or more); 32 x 8191 bf16 keys x 4 heads
-    // (128 items) 48.5, 47.5, 46.4, 49.8; 64 x 8192 tokens x 8 heads (512 items) 147, 139, 134, 140.
+    // Measured with two CTAs an SM, us at splits for 1, 2, 4 and 8 waves: one request of 131072 tokens x 4 heads (4 items)
+    // 31, 39, 56, 74; 8 x 2000 tokens x 8 heads (64 items) 15.4, 15.8, 15.7, 16.0 (19.6 at 32 tiles a CTA or more); 32 x 8191
+    // bf16 keys x 4 heads (128 items) 48.5, 47.5, 46.4, 49.8; 64 x 4096 to 8192 tokens x 8 heads (512 items) 147, 139, 134, 140.
     const int64_t slots = ctas_per_sm(d, p.tile_rows == 8, tile_keys == kCacheTileKeys) * kPlanSms;
     int64_t splits;
     if (4 * items <= slots) {

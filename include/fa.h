@@ -175,7 +175,8 @@ fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* k
                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * The paged 8-bit cache.  k_cache and v_cache are [n_blocks,Hk,block_size,d] arrays of e4m3 codes, k_scale and v_scale float [n_blocks,Hk]: a cached value is code * scale of its block and head.
+ * The paged 8-bit cache.  k_cache and v_cache are [n_blocks,Hk,block_size,d] arrays of e4m3 codes, k_scale and v_scale
+ * float [n_blocks,Hk]: a cached value is code * scale of its block and head.
  * block_size is 16, 32, 64 or 128, d 64 or 128.  A token's slot is block * block_size + its place in the block.
  * block_table is int [B,max_blocks]: token p of request b is in block block_table[b][p / block_size].
  *
@@ -252,11 +253,11 @@ void fa_debug_time_bwd_main(void* start_event, void* stop_event);
 /*
  * fa_test_force_wait_timeout — a switch for testing the failure path of the bounded device waits; the
  * pages have no counterpart.  With enable != 0, every later launch of the tensor-core kernels (fa_fwd,
- * fa_fwd_stepnorm, fa_bwd, fa_bwd_noalloc, fa_cross_fwd and fa_cache_fwd with many rows, fa_cross_bwd, from any thread) withholds its Q tile loads and gives its waits
- * a budget of about 10 ms instead of about 2 s, so that the first wait on Q runs out: the kernel winds down
- * by itself (no fault, no trap), fa_check_status() then reports FA_ERR_TIMEOUT, and the outputs of those
- * calls are not valid.  enable = 0 restores normal operation.  Off by default; nothing but an explicit call
- * (no environment variable) turns it on.
+ * fa_fwd_stepnorm, fa_bwd, fa_bwd_noalloc, fa_cross_fwd and fa_cache_fwd with many rows, fa_cross_bwd, from any
+ * thread) withholds its Q tile loads and gives its waits a budget of about 10 ms instead of about 2 s, so that the
+ * first wait on Q runs out: the kernel winds down by itself (no fault, no trap), fa_check_status() then reports
+ * FA_ERR_TIMEOUT, and the outputs of those calls are not valid.  enable = 0 restores normal operation.  Off by
+ * default; nothing but an explicit call (no environment variable) turns it on.
  */
 void fa_test_force_wait_timeout(int enable);
 
