@@ -9,7 +9,8 @@ from test_cache import _cache_case, _check_cache, _wide
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("wide", [False, True])
-@pytest.mark.parametrize("Hq,Hk,N,lens", [(4, 1, 150, [150, 149, 151, 700]), (2, 2, 300, [300, 0, 1, 431]), (3, 1, 129, [129, 128, 257, 64])])
+@pytest.mark.parametrize("Hq,Hk,N,lens", [(4, 1, 150, [150, 149, 151, 700]), (2, 2, 300, [300, 0, 1, 431]),
+                                          (3, 1, 129, [129, 128, 257, 64])])
 def test_prompts(Hq, Hk, N, lens, wide, d):
     """Prompts into an empty cache, shorter ones in the same call, and chunks behind earlier tokens."""
     fa = need_gpu()

@@ -83,7 +83,8 @@ def test_the_square_calls_outputs_come_from_the_given_stream(streams, monkeypatc
     x = torch.zeros(1, 1, 1, 64)
     monkeypatch.setattr(_Tensor, "is_cuda", True, raising=False)
     monkeypatch.setattr(_Tensor, "device", x.device, raising=False)
-    for call, outputs, others in ((lambda s: fa.fa_fwd(x, x, x, stream=s), 2, 0), (lambda s: fa.fa_fwd_f32(x, x, x, stream=s), 2, 0),
+    for call, outputs, others in ((lambda s: fa.fa_fwd(x, x, x, stream=s), 2, 0),
+                                  (lambda s: fa.fa_fwd_f32(x, x, x, stream=s), 2, 0),
                                   (lambda s: fa.fa_fwd_stepnorm(x, x, x, stream=s), 2, 0),
                                   (lambda s: fa.fa_bwd(x, x, x, x, x, x, stream=s), 3, 1),
                                   (lambda s: fa.fa_bwd_noalloc(x, x, x, x, x, x, stream=s), 3, 0)):
